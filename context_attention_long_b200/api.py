@@ -504,13 +504,23 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _on_stream(stream, *tensors):
-    """Tensors that a binding allocated for a call on another stream than the
-    current one, where the allocator would take them as free too early."""
-    if stream is not None and stream != torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _new(like, shape, dtype, stream, returned=True):
+    """A tensor that a binding allocates for a call on `stream` (None: the
+    current one): a block of that stream's pool.  The allocator hands a block
+    out again while the work that last used it may still be queued on the
+    pool's own stream, so a block of the current stream's pool could be written
+    by both streams at once.  `returned`: the caller will use it on the current
+    stream, and its block may not be handed out before that work either."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    current = torch.cuda.current_stream()
+    if stream == current:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if returned:
+        t.record_stream(current)
+    return t
 
 
 def _norm_rope_args(q, k, q_weight, k_weight, cos, sin, positions, device):
@@ -555,19 +565,15 @@ def cpattn_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos=None, sin=N
     device = torch.cuda.current_device()
     qp, qs, kp, ks, wq, wk, f32, cp, sp, pp, sizes = _norm_rope_args(q, k, q_weight, k_weight, cos, sin, positions,
                                                                      device)
-    made = []
     if q_out is None:
-        q_out = q.new_empty(q.shape)
-        made.append(q_out)
+        q_out = _new(q, q.shape, q.dtype, stream)
     if k_out is None and k is not None:
-        k_out = k.new_empty(k.shape)
-        made.append(k_out)
+        k_out = _new(k, k.shape, k.dtype, stream)
     qop, qos = _view(q_out, "q_out", device, q.shape)
     kop, kos = (None, None) if k is None else _view(k_out, "k_out", device, k.shape)
     _check(_native.load().cpattn_qk_norm_rope(qp, qs, kp, ks, wq, wk, f32, cp, sp, pp, qop, qos, kop, kos, *sizes,
                                               pos0, interleaved, eps, _raw_stream(stream, device)),
            "cpattn_qk_norm_rope")
-    _on_stream(stream, *made)
     return q_out, k_out
 
 
@@ -588,18 +594,12 @@ def cpattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=N
     D = q.shape[3]
     gqp, gqs = _view(dq_out, "dq_out", device, q.shape)
     gkp, gks = (None, None) if k is None else _view(dk_out, "dk_out", device, k.shape)
-    made = []
-
-    def new(shape, dtype):
-        made.append(q.new_empty(shape, dtype=dtype))
-        return made[-1]
-
-    dq = new(q.shape, q.dtype) if dq is None else dq
-    dk = new(k.shape, k.dtype) if dk is None and k is not None else dk
-    dqw = new((D,), q_weight.dtype) if want_weights and q_weight is not None else None
-    dkw = new((D,), k_weight.dtype) if want_weights and k_weight is not None and k is not None else None
+    dq = _new(q, q.shape, q.dtype, stream) if dq is None else dq
+    dk = _new(q, k.shape, k.dtype, stream) if dk is None and k is not None else dk
+    dqw = _new(q, (D,), q_weight.dtype, stream) if want_weights and q_weight is not None else None
+    dkw = _new(q, (D,), k_weight.dtype, stream) if want_weights and k_weight is not None and k is not None else None
     if workspace is None and (dqw is not None or dkw is not None):
-        workspace = new((cpattn_qk_norm_rope_backward_workspace_bytes(D),), torch.uint8)
+        workspace = _new(q, (cpattn_qk_norm_rope_backward_workspace_bytes(D),), torch.uint8, stream, returned=False)
     dqp, dqs = _view(dq, "dq", device, q.shape)
     dkp, dks = (None, None) if k is None else _view(dk, "dk", device, k.shape)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -607,7 +607,6 @@ def cpattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=N
         qp, qs, kp, ks, gqp, gqs, gkp, gks, wq, wk, f32, cp, sp, pp, dqp, dqs, dkp, dks,
         None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(), *sizes, pos0, interleaved,
         eps, _ptr(workspace), nbytes, _raw_stream(stream, device)), "cpattn_qk_norm_rope_backward")
-    _on_stream(stream, *made)
     return dq, dk, dqw, dkw
 
 
@@ -632,18 +631,14 @@ def cpattn_cross_attention(q, k, v, kv_lens=None, out=None, lse=None, want_lse=T
     device = torch.cuda.current_device()
     qp, qs, kp, ks, vp, vs, lp, sizes = _cross_args(q, k, v, kv_lens, device)
     B, H, _, Sq, _, _ = sizes
-    made = []
     if out is None:
-        out = q.new_empty(q.shape)
-        made.append(out)
+        out = _new(q, q.shape, q.dtype, stream)
     if lse is None and want_lse:
-        lse = q.new_empty((B, H, Sq), dtype=torch.float32)
-        made.append(lse)
+        lse = _new(q, (B, H, Sq), torch.float32, stream)
     op = _plain(out, "out", device, torch.bfloat16, q.shape)
     _check(_native.load().cpattn_cross_attention(qp, qs, kp, ks, vp, vs, op,
                                                  _plain(lse, "lse", device, torch.float32, (B, H, Sq)), lp, *sizes,
                                                  _raw_stream(stream, device)), "cpattn_cross_attention")
-    _on_stream(stream, *made)
     return out, lse
 
 
@@ -675,15 +670,9 @@ def cpattn_cross_attention_backward(q, k, v, out, lse, dout, kv_lens=None, dq=No
     device = torch.cuda.current_device()
     qp, qs, kp, ks, vp, vs, lp, sizes = _cross_args(q, k, v, kv_lens, device)
     B, H, Hk, Sq, Skv, D = sizes
-    made = []
-
-    def new(shape, dtype):
-        made.append(q.new_empty(shape, dtype=dtype))
-        return made[-1]
-
-    dq = new(q.shape, q.dtype) if dq is None else dq
-    dk = new(k.shape, k.dtype) if dk is None else dk
-    dv = new(v.shape, v.dtype) if dv is None else dv
+    dq = _new(q, q.shape, q.dtype, stream) if dq is None else dq
+    dk = _new(q, k.shape, k.dtype, stream) if dk is None else dk
+    dv = _new(q, v.shape, v.dtype, stream) if dv is None else dv
     if lse is None:
         raise ValueError("lse is required")
     ptrs = [_plain(t, name, device, torch.bfloat16, shape)
@@ -696,7 +685,7 @@ def cpattn_cross_attention_backward(q, k, v, out, lse, dout, kv_lens=None, dq=No
         while workspace is None:
             nbytes = cross_backward_workspace_bytes(B, H, Hk, Sq, Skv, D, budget)
             try:
-                workspace = new((nbytes,), torch.uint8)
+                workspace = _new(q, (nbytes,), torch.uint8, stream, returned=False)
             except torch.OutOfMemoryError:     # fewer pairs at once
                 if nbytes == least:
                     raise
@@ -704,7 +693,6 @@ def cpattn_cross_attention_backward(q, k, v, out, lse, dout, kv_lens=None, dq=No
     _check(_native.load().cpattn_cross_attention_backward(
         qp, qs, kp, ks, vp, vs, ptrs[0], sp, ptrs[1], lp, *ptrs[2:], *sizes, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _raw_stream(stream, device)), "cpattn_cross_attention_backward")
-    _on_stream(stream, *made)
     return dq, dk, dv
 
 

@@ -1,0 +1,100 @@
+"""What the operators' bindings do around the library calls, without a GPU: the
+library is replaced by one that accepts everything, and tensors by host tensors
+that note the stream whose pool they came from."""
+import contextlib
+
+import pytest
+import torch
+
+from context_attention_long_b200 import _native, api
+
+CURRENT, OTHER = "current stream", "other stream"
+
+
+class Library:
+    """Accepts every call; sizes of workspaces are small numbers."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 64 if name.endswith("_bytes") else 0
+        return call
+
+
+class Stream:
+    cuda_stream = 5
+
+    def __init__(self, name):
+        self.name = name
+
+    def __eq__(self, other):
+        return self.name == other.name
+
+
+class Host(torch.Tensor):
+    """A host tensor that the bindings take for a device tensor; `made`
+    collects what is allocated from it, with the pool it came from."""
+    made, active = [], [CURRENT]
+
+    def new_empty(self, shape, dtype=None):
+        t = torch.zeros(shape, dtype=dtype or self.dtype).as_subclass(Host)
+        t.pool, t.recorded = Host.active[-1], []
+        Host.made.append(t)
+        return t
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.name)
+
+
+@pytest.fixture()
+def host(monkeypatch):
+    lib = Library()
+
+    @contextlib.contextmanager
+    def on(stream):
+        Host.active.append(stream.name)
+        yield
+        Host.active.pop()
+
+    def address(t, *_):
+        return None if t is None else t.data_ptr()
+    monkeypatch.setattr(_native, "load", lambda: lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: Stream(Host.active[-1]))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(api, "_view", lambda t, *_: (address(t), None))
+    monkeypatch.setattr(api, "_plain", address)
+    monkeypatch.setattr(api, "_ptr", address)
+    monkeypatch.setattr(api, "_raw_stream", lambda stream, device: 0)
+    monkeypatch.setattr(Host, "made", [])
+    monkeypatch.setattr(Host, "active", [CURRENT])
+    return lib
+
+
+def _host(*shape, dtype=torch.bfloat16):
+    return torch.zeros(shape, dtype=dtype).as_subclass(Host)
+
+
+def _calls(stream):
+    q, k = _host(2, 3, 4, 64), _host(2, 5, 2, 64)
+    t, w = _host(2, 3, 2, 64), _host(64, dtype=torch.float32)
+    lse = _host(2, 4, 3, dtype=torch.float32)
+    return [lambda: api.cpattn_qk_norm_rope(q, t, w, w, stream=stream),
+            lambda: api.cpattn_qk_norm_rope_backward(q, t, q, t, w, w, stream=stream),
+            lambda: api.cpattn_cross_attention(q, k, k, stream=stream),
+            lambda: api.cpattn_cross_attention_backward(q, k, k, q, lse, q, stream=stream)]
+
+
+@pytest.mark.parametrize("i", range(4))
+@pytest.mark.parametrize("stream", [None, Stream(CURRENT), Stream(OTHER)])
+def test_allocations_come_from_the_pool_of_the_launch_stream(host, i, stream):
+    returned = _calls(stream)[i]()
+    pool = CURRENT if stream is None else stream.name
+    assert Host.made and all(t.pool == pool for t in Host.made)
+    # what the caller reads on the current stream is noted as used there
+    for t in Host.made:
+        seen = any(t is r for r in returned)
+        assert t.recorded == ([CURRENT] if pool == OTHER and seen else [])
