@@ -129,7 +129,9 @@ struct NormAngles {
         for (int i = 0; i < kN; ++i) sn[i] = -sn[i];
       }
     } else {
-      const float one = turned ? __int_as_float(0x7fffffff) : 1.f;
+      // a piece behind the rotated part, or a position outside the table: NaN
+      // over its whole row, the pieces behind the rotated part too
+      const float one = inside ? 1.f : __int_as_float(0x7fffffff);
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         cs[i] = one;

@@ -567,8 +567,9 @@ int cpattn_ulysses_attention_backward(const void *q, const void *k, const void *
  *                not read; no rotation).  Angles are the caller's, so that
  *                they can be computed in any precision.
  *   positions    int32 [B, S] device: the table row of each token; NULL: token
- *                s uses row pos0 + s.  A position outside [0, n_pos) gives a
- *                row of NaN and sets bit 7 of the device status word.
+ *                s uses row pos0 + s.  A position outside [0, n_pos) makes the
+ *                token's rows NaN, their elements behind rotary_dim too, and
+ *                sets bit 7 of the device status word.
  *   q_out, k_out may be q and k themselves (with the same strides); no other
  *                overlap of inputs and outputs is allowed.
  *   rotary_dim   a multiple of 16, 0 .. D.  D is 64 or 128.
@@ -599,6 +600,8 @@ int cpattn_qk_norm_rope(const void *q, const long long *q_strides, const void *k
  *                    wanted.  Overwritten; calls that overlap on the GPU need
  *                    one each.
  * The weight gradients are added in a fixed order: the same bytes every run.
+ * A position outside the table makes the token's rows of dq and dk and all of
+ * dq_weight and dk_weight NaN, and sets the status bit as in the forward.
  * Other arguments and errors as cpattn_qk_norm_rope, and WORKSPACE.
  */
 size_t cpattn_qk_norm_rope_backward_workspace_bytes(int D);
