@@ -71,6 +71,32 @@ def _readable(t):
     return t if ok else t.clone(memory_format=torch.contiguous_format)   # contiguous() keeps an unaligned address
 
 
+class _FirstOrderOnly(torch.autograd.Function):
+    """Passes a backward's gradients on as functions of `inputs` whose own
+    gradient raises."""
+
+    @staticmethod
+    def forward(ctx, name, n, *tensors):
+        ctx.name, ctx.n = name, n
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name}: gradients of its gradients are not offered")
+
+
+def _first_order_only(name, grads, *inputs):
+    """The gradients that a backward returns.  Where autograd records it
+    (create_graph=True) they would be constants to a loss of them, which would
+    lose that part of its gradient without a word; so they are made functions of
+    all that the backward read, and differentiating them raises."""
+    if not torch.is_grad_enabled():
+        return grads
+    there = [g for g in grads if g is not None]
+    passed = iter(_FirstOrderOnly.apply(name, len(there), *there, *(t for t in inputs if t is not None)))
+    return tuple(None if g is None else next(passed) for g in grads)
+
+
 class QKNormRopeFunction(torch.autograd.Function):
     """Per-head RMS norm of Q and K with the position rotation.  The backward
     needs only the forward's inputs."""
@@ -89,14 +115,16 @@ class QKNormRopeFunction(torch.autograd.Function):
         dq, dk, dqw, dkw = api.cpattn_qk_norm_rope_backward(
             q, k, _readable(dq_out), None if k is None else _readable(dk_out), q_weight, k_weight, cos, sin,
             positions, eps, interleaved, pos0, want_weights=any(ctx.needs_input_grad[2:4]))
-        return (dq, dk, dqw, dkw) + (None,) * 6
+        return _first_order_only("qk_norm_rope", (dq, dk, dqw, dkw), dq_out, dk_out, q, k, q_weight, k_weight) + \
+            (None,) * 6
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
                  interleaved=True, pos0=0):
     """Differentiable per-head RMS norm of q (B, S, H, D) and k (B, S, Hk, D)
     with the position rotation (api.cpattn_qk_norm_rope); returns (q, k).
-    Gradients go to q, k and the weights, not to the tables."""
+    Gradients go to q, k and the weights, not to the tables; first-order only:
+    differentiating them (create_graph=True) raises."""
     return QKNormRopeFunction.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved, pos0)
 
 
@@ -115,12 +143,13 @@ class CrossAttentionFunction(torch.autograd.Function):
         dout = dout.contiguous()
         dq, dk, dv = api.cpattn_cross_attention_backward(q, k, v, out, lse,
                                                          dout if dout.data_ptr() % 16 == 0 else dout.clone(), kv_lens)
-        return dq, dk, dv, None
+        return _first_order_only("cross_attention", (dq, dk, dv), dout, q, k, v) + (None,)
 
 
 def cross_attention(q, k, v, kv_lens=None):
     """Differentiable cross attention of q (B, Sq, H, D) to k, v
-    (B, Skv, Hk, D) (api.cpattn_cross_attention); returns out (B, Sq, H, D)."""
+    (B, Skv, Hk, D) (api.cpattn_cross_attention); returns out (B, Sq, H, D).
+    First-order gradients only: differentiating them (create_graph=True) raises."""
     return CrossAttentionFunction.apply(q, k, v, kv_lens)
 
 
