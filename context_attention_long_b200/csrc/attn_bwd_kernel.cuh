@@ -110,10 +110,12 @@ __device__ __forceinline__ uint32_t bwd_dq_dp_col(int b) { return b ? 384u : 128
 // before it reduces any of them, so that many rows' loads are in flight at
 // once.  The sum order is fixed: the result is deterministic.
 constexpr int kDeltaPasses = 4;
-__global__ void __launch_bounds__(256, 3) attn_bwd_delta_kernel(const __nv_bfloat16 *__restrict__ out,
-                                                                const __nv_bfloat16 *__restrict__ dout,
-                                                                float *__restrict__ delta, int B, int S, int H,
-                                                                int D) {
+// Rows of batch elements for which skip(b) holds are not written, and passes
+// over such rows alone (skip_all(first, last)) not read.
+template <class Skip, class SkipAll>
+__device__ __forceinline__ void bwd_delta_rows(const __nv_bfloat16 *__restrict__ out,
+                                               const __nv_bfloat16 *__restrict__ dout, float *__restrict__ delta,
+                                               int B, int S, int H, int D, Skip skip, SkipAll skip_all) {
   // Rows are (token, head) pairs, B*S*H < 2^31 (checked on the host).
   const int lane = threadIdx.x & 31;
   const int lpr = D >> 3;                    // lanes per row (16 for D = 128, 8 for D = 64)
@@ -124,6 +126,7 @@ __global__ void __launch_bounds__(256, 3) attn_bwd_delta_kernel(const __nv_bfloa
   const unsigned nrows = static_cast<unsigned>(B) * S * H;
   const unsigned per_iter = static_cast<unsigned>(rpp) * kDeltaPasses;
   for (unsigned r0 = warp * per_iter; r0 < nrows; r0 += nwarps * per_iter) {
+    if (skip_all(r0, min(r0 + per_iter, nrows) - 1)) continue;
     uint4 ov[kDeltaPasses], gv[kDeltaPasses];
 #pragma unroll
     for (int u = 0; u < kDeltaPasses; ++u) {
@@ -164,10 +167,16 @@ __global__ void __launch_bounds__(256, 3) attn_bwd_delta_kernel(const __nv_bfloa
             ++b;
           }
         }
-        delta[(static_cast<size_t>(b) * H + h) * S + s] = acc;
+        if (!skip(b)) delta[(static_cast<size_t>(b) * H + h) * S + s] = acc;
       }
     }
   }
+}
+__global__ void __launch_bounds__(256, 3) attn_bwd_delta_kernel(const __nv_bfloat16 *__restrict__ out,
+                                                                const __nv_bfloat16 *__restrict__ dout,
+                                                                float *__restrict__ delta, int B, int S, int H,
+                                                                int D) {
+  bwd_delta_rows(out, dout, delta, B, S, H, D, [](unsigned) { return false; }, [](unsigned, unsigned) { return false; });
 }
 
 // Units: (problem, b, h, 128-row tile) over the problem's heads [h0, h0 + nh),

@@ -1,11 +1,13 @@
 // cross_bwd_kernel.cuh -- gradient of cross attention for sm_100a.
 //
 // Per (batch element, query head), over the valid states, with P recomputed
-// from the forward's LSE and Delta = rowsum(dO * O) (attn_bwd_delta_kernel):
+// from the forward's LSE and Delta = rowsum(dO * O):
 //   dS = P * (dO V^T - Delta),  dQ = dS K * scale,
 //   dV = sum over the group's heads of P^T dO,  dK = the same sum of dS^T Q * scale.
 // The products, their TMEM layout and the dS tiles are those of
 // attn_bwd_kernel.cuh.  What differs:
+//   - Delta of elements with few states is summed from P and dP, since the saved
+//     output is rounded (cross_delta_kernel).
 //   - dK/dV: an encoder's states are few tiles and the queries many, so one CTA
 //     a K/V tile would leave most SMs idle or unevenly loaded.  The walks of
 //     all valid tiles -- every Q tile of every head of its group -- are laid
@@ -31,6 +33,7 @@
 #include "operators_internal.h"
 #include "operators_ptx.cuh"
 #include "cross_kernel.cuh"
+#include "cross_token_kernel.cuh"
 
 namespace cpattn {
 
@@ -151,6 +154,127 @@ __device__ __forceinline__ long long cross_total_steps(const CrossBwdParams &p, 
     for (int k = 0; k < p.k_tiles; ++k) tiles += static_cast<long long>(ends[k]) * (k + 1);
   }
   return tiles * p.walk;
+}
+
+// ==================================================================== Delta
+// rowsum(dO * O) as attn_bwd_delta_kernel, except for elements of at most
+// kCrossFewStates states.  The forward's output was rounded to bf16 and made
+// with P rounded to bf16, which puts a common error into all of a row's
+// dP - Delta; over n states it is some 1 / sqrt(n) of the roundings of P and dS
+// themselves.  In dQ and dK, normal data, that error and theirs together are
+// 0.0044 of the gradient at 2 states, 0.0038 at 3, 0.0026 at 16 and 0.0025 at
+// 32, theirs alone 0.0023.  So few states take Delta by its definition,
+// sum_j P_j dP_j, in float32.  Bound by the reads of q and dO, as the other is by out and dO:
+// a warp takes 16 rows (queries of all heads of a group) by mma.m16n8k16
+// against K and V in shared memory, loaded once a chunk of rows.  A fragment's k
+// index may be any order of the head's elements, the same for both operands: a
+// lane's are eight consecutive ones of each 32, so that all loads are 16 bytes.
+// The whole backward, 32760 queries of 40 heads of 128, takes 519 us with 8
+// states and 535 with 32, where rowsum(dO * O) took 524 and 518 (K and V from
+// L1 557 and 639; the loads of one piece at a time 560 and 577); heads of 64,
+// 8192 queries x 4, 32 / 8 heads, 303 against 277.
+//   kMany: elements may also have more states; three CTAs an SM for the row
+// sums, whose registers leave room for one piece's loads.
+constexpr int kCrossFewStates = 32;
+template <int D, bool kMany>
+__global__ void __launch_bounds__(256, kMany ? 3 : 2) cross_delta_kernel(const __grid_constant__ CrossDeltaParams p) {
+  auto len_of = [&](int b) { return p.kv_lens == nullptr ? p.Skv : max(0, min(p.Skv, __ldg(p.kv_lens + b))); };
+  if constexpr (kMany)
+    bwd_delta_rows(p.out, p.dout, p.delta, p.B, p.Sq, p.H, D,
+                   [&](unsigned b) { return len_of(static_cast<int>(b)) <= kCrossFewStates; },
+                   [&](unsigned r0, unsigned r1) {
+                     const int b0 = p.by_element.div(static_cast<int>(r0)), b1 = p.by_element.div(static_cast<int>(r1));
+                     return b0 == b1 && len_of(b0) <= kCrossFewStates;
+                   });
+  // K and V of a chunk's states in the order of the operands: [K, V][eight
+  // states][32 elements of the head][lane]
+  constexpr int kC = D / 32, kN = kCrossFewStates / 8;
+  constexpr int kLoads = kMany ? 1 : kC;     // 32-element pieces loaded before any is used
+  __shared__ uint4 kv[2][kN][kC][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
+  const int group = p.H / p.Hk, rows = group * p.Sq;
+  const unsigned chunks = static_cast<unsigned>(p.B) * p.Hk * p.chunks;
+  for (unsigned u = blockIdx.x; u < chunks; u += gridDim.x) {
+    // the key heads of the same queries next to each other: their rows are in DRAM
+    const int bc = p.by_hk.div(static_cast<int>(u)), hk = static_cast<int>(u) - bc * p.Hk;
+    const int b = p.by_chunks.div(bc), chunk = bc - b * p.chunks, len = len_of(b);
+    if (len > kCrossFewStates) continue;
+    __syncthreads();                         // the last chunk's K and V have been read
+    for (int i = threadIdx.x; i < 2 * kN * kC * 32; i += 256) {
+      const int j = (i / (kC * 32)) % kN * 8 + (i & 31) / 4, e = i / 32 % kC * 32 + (i & 3) * 8;
+      const bool is_v = i >= kN * kC * 32;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (j < len)
+        x = *reinterpret_cast<const uint4 *>(is_v ? p.v + b * p.vb + hk * p.vh + j * p.vs + e
+                                                  : p.k + b * p.kb + hk * p.kh + j * p.ks + e);
+      (&kv[0][0][0][0])[i] = x;
+    }
+    __syncthreads();
+    const int end = min(p.blocks, (chunk + 1) * p.chunk_blocks);
+    for (int block = chunk * p.chunk_blocks + warp; block < end; block += 8) {
+      bool there[2];                         // this lane's rows lane / 4 and lane / 4 + 8 of the block
+      size_t at[2];                          // their place in LSE and Delta
+      const __nv_bfloat16 *q[2], *g[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = block * 16 + (lane >> 2) + 8 * i;
+        there[i] = r < rows;
+        const int s = p.by_group.div(there[i] ? r : 0), h = hk * group + (there[i] ? r : 0) - s * group;
+        at[i] = (static_cast<size_t>(b) * p.H + h) * p.Sq + s;
+        q[i] = p.q + b * p.qb + s * p.qs + h * p.qh + 8 * t;
+        g[i] = p.dout + ((static_cast<size_t>(b) * p.Sq + s) * p.H + h) * D + 8 * t;
+      }
+      float s[kN][4], dp[kN][4];
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = dp[n][e] = 0.f;
+#pragma unroll
+      for (int c0 = 0; c0 < kC; c0 += kLoads) {
+        uint4 xs[kLoads][2], ys[kLoads][2];
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            xs[c][i] = ys[c][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (there[i]) {
+              xs[c][i] = __ldcs(reinterpret_cast<const uint4 *>(q[i] + 32 * (c0 + c)));
+              ys[c][i] = __ldcs(reinterpret_cast<const uint4 *>(g[i] + 32 * (c0 + c)));
+            }
+          }
+#pragma unroll
+        for (int c = 0; c < kLoads; ++c) {
+          const uint4 (&x)[2] = xs[c], (&y)[2] = ys[c];
+          const uint32_t xa[4] = {x[0].x, x[1].x, x[0].y, x[1].y}, xb[4] = {x[0].z, x[1].z, x[0].w, x[1].w};
+          const uint32_t ya[4] = {y[0].x, y[1].x, y[0].y, y[1].y}, yb[4] = {y[0].z, y[1].z, y[0].w, y[1].w};
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            if (8 * n >= len) break;           // (the same for the whole warp)
+            const uint4 kk = kv[0][n][c0 + c][lane], vv = kv[1][n][c0 + c][lane];
+            mma_16n8k16(s[n], xa, kk.x, kk.y);
+            mma_16n8k16(s[n], xb, kk.z, kk.w);
+            mma_16n8k16(dp[n], ya, vv.x, vv.y);
+            mma_16n8k16(dp[n], yb, vv.z, vv.w);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float lse = there[i] ? __ldg(p.lse + at[i]) : INFINITY;
+        const float l2 = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;   // -inf: the row saw nothing
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (8 * n + 2 * t + e < len)
+              sum = fmaf(ex2_approx(fmaf(s[n][2 * i + e], p.scale_log2, -l2)), dp[n][2 * i + e], sum);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (t == 0 && there[i]) p.delta[at[i]] = sum;
+      }
+    }
+  }
 }
 
 // =================================================================== dK, dV

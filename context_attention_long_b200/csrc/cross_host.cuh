@@ -196,6 +196,52 @@ static size_t cross_partial_bytes(int B, int H, int Hk, int Sq, int Skv, int D) 
   return static_cast<size_t>(runs) * 2 * 2 * 128 * D * sizeof(float);
 }
 
+// Delta: the self-attention's row sums where no element can have few states,
+// else the kernel that tells the elements apart.
+static cudaError_t launch_cross_delta(const CrossBwdParams &p, const void *q, const View4 &vq, const void *k,
+                                      const View4 &vk, const void *v, const View4 &vv, const void *out,
+                                      const void *dout, float *delta, int D, cudaStream_t stream) {
+  if (p.kv_lens == nullptr && p.Skv > kCrossFewStates) return launch_bwd_delta(out, dout, delta, p.B, p.Sq, p.H, D, stream);
+  CrossDeltaParams d;
+  std::memset(&d, 0, sizeof(d));
+  d.q = static_cast<const __nv_bfloat16 *>(q);
+  d.k = static_cast<const __nv_bfloat16 *>(k);
+  d.v = static_cast<const __nv_bfloat16 *>(v);
+  d.qb = vq.b; d.qs = vq.s; d.qh = vq.h;
+  d.kb = vk.b; d.ks = vk.s; d.kh = vk.h;
+  d.vb = vv.b; d.vs = vv.s; d.vh = vv.h;
+  d.out = static_cast<const __nv_bfloat16 *>(out);
+  d.dout = static_cast<const __nv_bfloat16 *>(dout);
+  d.lse = p.lse;
+  d.delta = delta;
+  d.kv_lens = p.kv_lens;
+  d.B = p.B;
+  d.Sq = p.Sq;
+  d.Skv = p.Skv;
+  d.H = p.H;
+  d.Hk = p.Hk;
+  const int group = p.H / p.Hk;
+  d.blocks = static_cast<int>((static_cast<long long>(group) * p.Sq + 15) / 16);
+  const bool many = p.Skv > kCrossFewStates;
+  const int ctas = (many ? 3 : 2) * std::max(device_sm_count(), 1);   // resident at once
+  // A chunk is at least a block a warp, and at most eight: enough rows for the
+  // chunk's K and V to be a small part of what is read.
+  const long long blocks = static_cast<long long>(p.B) * p.Hk * d.blocks;
+  d.chunk_blocks = 8 * static_cast<int>(std::min(8ll, std::max(1ll, blocks / (8ll * ctas))));
+  d.chunks = (d.blocks + d.chunk_blocks - 1) / d.chunk_blocks;
+  d.by_chunks.set(d.chunks);
+  d.by_hk.set(p.Hk);
+  d.by_group.set(group);
+  d.by_element.set(p.H * p.Sq);
+  d.scale_log2 = p.scale_log2;
+  const int grid = static_cast<int>(std::min<long long>(static_cast<long long>(p.B) * p.Hk * d.chunks, ctas));
+  if (D == 128)
+    (many ? cross_delta_kernel<128, true> : cross_delta_kernel<128, false>)<<<grid, 256, 0, stream>>>(d);
+  else
+    (many ? cross_delta_kernel<64, true> : cross_delta_kernel<64, false>)<<<grid, 256, 0, stream>>>(d);
+  return cudaGetLastError();
+}
+
 template <int D>
 static cudaError_t launch_cross_bwd_d(CrossBwdParams &p, cudaStream_t stream) {
   static std::mutex mu;
@@ -383,7 +429,7 @@ int cpattn_cross_attention_backward(const void *q, const long long *q_strides, c
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
   p.scale_log2 = static_cast<float>((1.0 / std::sqrt(static_cast<double>(D))) * 1.4426950408889634);
   p.timeout_ns = wait_timeout_ns();
-  if (cudaError_t e = launch_bwd_delta(out, dout, delta, B, Sq, H, D, stream); e != cudaSuccess)
+  if (cudaError_t e = launch_cross_delta(p, q, vq, k, vk, v, vv, out, dout, delta, D, stream); e != cudaSuccess)
     return cuda_fail(e, "cross attention backward launch");
   // Pairs whose dS fits together share the launches; the stream orders the
   // next group after the product that read this one's dS.

@@ -91,6 +91,20 @@ struct alignas(64) CrossTokenParams {
   float scale_log2;
   unsigned long long timeout_ns;
 };
+// Row sums Delta of the gradient.
+struct CrossDeltaParams {
+  const __nv_bfloat16 *q, *k, *v;        // [B, rows, heads, D] views, strides in elements
+  long long qb, qs, qh, kb, ks, kh, vb, vs, vh;
+  const __nv_bfloat16 *out, *dout;       // [B, Sq, H, D]
+  const float *lse;                      // [B, H, Sq]
+  float *delta;
+  const int *kv_lens;
+  int B, Sq, Skv, H, Hk;
+  int blocks;                            // 16-row blocks of a key head's query rows
+  int chunk_blocks, chunks;              // of them a CTA at a time, chunks of a key head
+  FastDiv by_chunks, by_hk, by_group, by_element;   // (by_element: H * Sq rows)
+  float scale_log2;
+};
 // Its gradient over the (batch element, key head) pairs [bh0, bh0 + n_bh).
 struct alignas(64) CrossBwdParams {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;   // 4-D maps as above

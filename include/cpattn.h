@@ -657,6 +657,9 @@ int cpattn_cross_attention(const void *q, const long long *q_strides, const void
  *                   cpattn_cross_attention_backward_ds_bytes() lets one more
  *                   of the B * Hk pairs share the launches.  Overwritten;
  *                   calls that overlap on the GPU need one each.
+ * rowsum(dout * out) is taken from the rounded out, except for elements of at
+ * most 32 states, where that would be the largest error: there it is summed from
+ * P and dout V^T.
  * All sums are added in a fixed order: the same bytes every run.  Other
  * arguments and errors as cpattn_cross_attention, SHAPE also for
  * Skv > 2^20, and WORKSPACE.
