@@ -660,13 +660,32 @@ def cross_backward_workspace_bytes(B, H, Hk, Sq, Skv, D, ds_budget=None) -> int:
     return cpattn_cross_attention_backward_workspace_bytes(B, H, Hk, Sq, Skv, D) + more * pair
 
 
+# Scratch up to here is allocated without asking for the device's free memory, a
+# question of some 70 us of host time: a step with more takes longer on the GPU
+# than it does on the host, the question included.
+_CROSS_DS_UNASKED = 256 << 20
+
+
+def _cross_allocation_budget(device, every, ds_budget):
+    """The dS budget for a workspace the cross-attention backward's binding
+    allocates itself (`every`: dS of all pairs): the given one, or by default
+    BACKWARD_DS_BUDGET, what exceeds _CROSS_DS_UNASKED capped at half the
+    device's free memory."""
+    if ds_budget is not None:
+        return int(ds_budget)
+    if min(every, BACKWARD_DS_BUDGET) <= _CROSS_DS_UNASKED:
+        return BACKWARD_DS_BUDGET
+    free, _ = torch.cuda.mem_get_info(device)
+    return min(BACKWARD_DS_BUDGET, max(_CROSS_DS_UNASKED, free // 2))
+
+
 def cpattn_cross_attention_backward(q, k, v, out, lse, dout, kv_lens=None, dq=None, dk=None, dv=None, workspace=None,
                                     stream=None, ds_budget=None):
     """Gradient of cpattn_cross_attention from the forward's output and LSE;
     returns (dq, dk, dv), contiguous bf16.  An allocated workspace holds up to
-    ds_budget bytes of dS scratch (default BACKWARD_DS_BUDGET; halved where the
-    device's memory does not allow it), and at least one (batch element, key
-    head) pair's."""
+    ds_budget bytes of dS scratch (default BACKWARD_DS_BUDGET, capped at half the
+    device's free memory where it is more than 256 MB; halved where memory does
+    not allow it), and at least one (batch element, key head) pair's."""
     device = torch.cuda.current_device()
     qp, qs, kp, ks, vp, vs, lp, sizes = _cross_args(q, k, v, kv_lens, device)
     B, H, Hk, Sq, Skv, D = sizes
@@ -680,7 +699,8 @@ def cpattn_cross_attention_backward(q, k, v, out, lse, dout, kv_lens=None, dq=No
                                    (dk, "dk", k.shape), (dv, "dv", k.shape))]
     sp = _plain(lse, "lse", device, torch.float32, (B, H, Sq))
     if workspace is None:
-        budget = BACKWARD_DS_BUDGET if ds_budget is None else int(ds_budget)
+        budget = _cross_allocation_budget(device, B * Hk * cpattn_cross_attention_backward_ds_bytes(H, Hk, Sq, Skv),
+                                          ds_budget)
         least = cross_backward_workspace_bytes(B, H, Hk, Sq, Skv, D, 0)
         while workspace is None:
             nbytes = cross_backward_workspace_bytes(B, H, Hk, Sq, Skv, D, budget)

@@ -40,7 +40,7 @@ class Host(torch.Tensor):
     made, active = [], [CURRENT]
 
     def new_empty(self, shape, dtype=None):
-        t = torch.zeros(shape, dtype=dtype or self.dtype).as_subclass(Host)
+        t = torch.empty(shape, dtype=dtype or self.dtype).as_subclass(Host)
         t.pool, t.recorded = Host.active[-1], []
         Host.made.append(t)
         return t
@@ -98,3 +98,26 @@ def test_allocations_come_from_the_pool_of_the_launch_stream(host, i, stream):
     for t in Host.made:
         seen = any(t is r for r in returned)
         assert t.recorded == ([CURRENT] if pool == OTHER and seen else [])
+
+
+MB = 1 << 20
+
+
+@pytest.mark.parametrize("pair,free,ds_budget,pairs", [
+    (200 * MB, 100 << 30, None, 4),          # all there is
+    (200 * MB, 1000 * MB, None, 2),          # within half of what is free
+    (200 * MB, 300 * MB, None, 1),           # half is less than what is taken unasked: 256 MB, one pair
+    (200 * MB, 1000 * MB, 800 * MB, 4),      # the caller's own budget
+    (200 * MB, 1000 * MB, 0, 1),
+    (64 * MB, None, None, 4),                # 256 MB in all: the free memory is not asked for
+])
+def test_scratch_of_the_cross_backward_leaves_free_memory(host, monkeypatch, pair, free, ds_budget, pairs):
+    def mem_get_info(device):
+        assert free is not None
+        return free, 180 << 30
+    monkeypatch.setattr(torch.cuda, "mem_get_info", mem_get_info)
+    monkeypatch.setattr(api, "cpattn_cross_attention_backward_ds_bytes", lambda *_: pair)
+    monkeypatch.setattr(api, "cpattn_cross_attention_backward_workspace_bytes", lambda *_: 1000 + pair)
+    q, k, lse = _host(2, 3, 4, 64), _host(2, 5, 2, 64), _host(2, 4, 3, dtype=torch.float32)
+    api.cpattn_cross_attention_backward(q, k, k, q, lse, q, ds_budget=ds_budget)
+    assert [t.numel() for t in Host.made if t.dtype is torch.uint8] == [1000 + pairs * pair]
