@@ -652,8 +652,9 @@ def cpattn_cross_attention_backward_workspace_bytes(B, H, Hk, Sq, Skv, D) -> int
 
 def cross_backward_workspace_bytes(B, H, Hk, Sq, Skv, D, ds_budget=None) -> int:
     """Bytes of the workspace the cross-attention backward's binding
-    allocates: the minimum, plus dS of further (batch element, key head) pairs
-    within ds_budget (default BACKWARD_DS_BUDGET)."""
+    allocates: the minimum, which holds dS of one (batch element, key head) pair
+    whatever the budget (2 bytes a query, state and head of the group), plus dS
+    of further pairs within ds_budget (default BACKWARD_DS_BUDGET)."""
     pair = cpattn_cross_attention_backward_ds_bytes(H, Hk, Sq, Skv)
     budget = BACKWARD_DS_BUDGET if ds_budget is None else int(ds_budget)
     more = max(0, min(B * Hk, budget // pair if pair else 0) - 1)

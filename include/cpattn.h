@@ -653,7 +653,10 @@ int cpattn_cross_attention(const void *q, const long long *q_strides, const void
  *   workspace       device, any alignment, at least
  *                   cpattn_cross_attention_backward_workspace_bytes(): row sums,
  *                   float32 partial sums of dK and dV, and dS of one (batch
- *                   element, key head) pair.  Each further
+ *                   element, key head) pair, which is the least there is: 2
+ *                   bytes a (query, state) of each of its H / Hk heads, both
+ *                   lengths rounded up to 128 (17 GB for 32 / 4 heads, 32768
+ *                   queries and as many states).  Each further
  *                   cpattn_cross_attention_backward_ds_bytes() lets one more
  *                   of the B * Hk pairs share the launches.  Overwritten;
  *                   calls that overlap on the GPU need one each.
