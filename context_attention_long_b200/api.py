@@ -650,15 +650,21 @@ def cpattn_cross_attention_backward_workspace_bytes(B, H, Hk, Sq, Skv, D) -> int
     return int(_native.load().cpattn_cross_attention_backward_workspace_bytes(B, H, Hk, Sq, Skv, D))
 
 
+# dS that the least workspace of the cross-attention backward holds: a pair's, or
+# this much of it (kCrossLeastDs of the library).
+_CROSS_DS_LEAST = 256 << 20
+
+
 def cross_backward_workspace_bytes(B, H, Hk, Sq, Skv, D, ds_budget=None) -> int:
     """Bytes of the workspace the cross-attention backward's binding
-    allocates: the minimum, which holds dS of one (batch element, key head) pair
-    whatever the budget (2 bytes a query, state and head of the group), plus dS
-    of further pairs within ds_budget (default BACKWARD_DS_BUDGET)."""
+    allocates: dS of as many (batch element, key head) pairs as fit ds_budget
+    (default BACKWARD_DS_BUDGET); of a part of one pair where it does not fit,
+    but at least of a pair or 256 MB; and the rest."""
     pair = cpattn_cross_attention_backward_ds_bytes(H, Hk, Sq, Skv)
     budget = BACKWARD_DS_BUDGET if ds_budget is None else int(ds_budget)
-    more = max(0, min(B * Hk, budget // pair if pair else 0) - 1)
-    return cpattn_cross_attention_backward_workspace_bytes(B, H, Hk, Sq, Skv, D) + more * pair
+    least = min(pair, _CROSS_DS_LEAST)
+    ds = min(B * Hk, budget // pair) * pair if 0 < pair <= budget else max(budget, least)
+    return cpattn_cross_attention_backward_workspace_bytes(B, H, Hk, Sq, Skv, D) + max(0, ds - least)
 
 
 # Scratch up to here is allocated without asking for the device's free memory, a
@@ -686,7 +692,8 @@ def cpattn_cross_attention_backward(q, k, v, out, lse, dout, kv_lens=None, dq=No
     returns (dq, dk, dv), contiguous bf16.  An allocated workspace holds up to
     ds_budget bytes of dS scratch (default BACKWARD_DS_BUDGET, capped at half the
     device's free memory where it is more than 256 MB; halved where memory does
-    not allow it), and at least one (batch element, key head) pair's."""
+    not allow it), and at least 256 MB or one (batch element, key head) pair's;
+    a pair that does not fit is done in ranges of its queries."""
     device = torch.cuda.current_device()
     qp, qs, kp, ks, vp, vs, lp, sizes = _cross_args(q, k, v, kv_lens, device)
     B, H, Hk, Sq, Skv, D = sizes

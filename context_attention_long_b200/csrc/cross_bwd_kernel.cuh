@@ -24,6 +24,10 @@
 //   - dQ: the persistent product over the stored dS with Sq x Skv tiles.  Rows
 //     of K behind the length meet dS = 0; they are zeroed in shared memory,
 //     since they may hold NaN.
+//   - A pair whose dS exceeds the scratch is done in ranges of its walk, one
+//     after the other; their dK and dV are added in float32 (cross_range_kernel).
+//     32768 queries of 32 / 4 heads of 128 against as many states, 17 GB of dS a
+//     pair: 51 ms in ranges of 1 to 8 GB, as whole, and 77 in ranges of 256 MB.
 //   - Gradients of states behind the length are zeros: those of a partly valid
 //     tile come out of the products so, those of other tiles are written beside
 //     the dQ product.
@@ -41,11 +45,10 @@ __device__ __forceinline__ int cross_bwd_len(const CrossBwdParams &p, int b) {
   return p.kv_lens == nullptr ? p.Skv : max(0, min(p.Skv, __ldg(p.kv_lens + b)));
 }
 
-// Byte offset of the dS tile of pair bh (counted from p.bh0), head hg of its
-// group, Q tile qt and K tile kt.
-__device__ __forceinline__ size_t cross_ds_tile(const CrossBwdParams &p, int bh_local, int hg, int qt, int kt) {
-  const int group = p.H / p.Hk;
-  return (((static_cast<size_t>(bh_local) * group + hg) * p.q_tiles + qt) * p.k_tiles + kt) * kBwdDsTileBytes;
+// Byte offset of the dS tile of pair bh (counted from p.bh0), step w of its walk
+// and K tile kt.
+__device__ __forceinline__ size_t cross_ds_tile(const CrossBwdParams &p, int bh_local, int w, int kt) {
+  return ((static_cast<size_t>(bh_local) * p.walk + w) * p.k_tiles + kt) * kBwdDsTileBytes;
 }
 
 // The walks of the valid tiles end to end, in (K tile, pair, Q tile) order, and
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_bwd_dkv_kernel(const __g
           tma_load_4d(sb + L::kOffA + hf * L::kBoxBytes, &p.tm_k, hf * 64, R.hk, R.kt * 128, R.b, sb + BAR_KV);
           tma_load_4d(sb + L::kOffB + hf * L::kBoxBytes, &p.tm_v, hf * 64, R.hk, R.kt * 128, R.b, sb + BAR_KV);
         }
-        int hg = p.by_q_tiles.div(R.w), qt = R.w - hg * p.q_tiles;
+        int hg = p.by_q_tiles.div(p.w0 + R.w), qt = p.w0 + R.w - hg * p.q_tiles;
         for (int j = 0; j < R.n; ++j, ++i) {
           const int qs = i % QS, os = i % OS;
           const int h = R.hk * group + hg;
@@ -508,8 +511,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_bwd_dkv_kernel(const __g
     int vw = R.w;
     float nl = INFINITY, nd = 0.f;
     auto load_vec = [&]() {          // of the next walk step in turn
-      const int hg = p.by_q_tiles.div(vw);
-      const int q = (vw - hg * p.q_tiles) * 128 + row;
+      const int hg = p.by_q_tiles.div(p.w0 + vw);
+      const int q = (p.w0 + vw - hg * p.q_tiles) * 128 + row;
       const size_t at = (static_cast<size_t>(V.b) * p.H + V.hk * group + hg) * p.Sq + q;
       nl = INFINITY;
       nd = 0.f;
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_bwd_dkv_kernel(const __g
     int i = 0, seg = 0;
     for (; ok && R.left > 0; R.next(p), ++seg) {
       const bool seen = row < R.len - R.kt * 128;   // a state behind the length: P and dS exactly 0
-      unsigned char *ds_dst = p.ds + cross_ds_tile(p, R.bh_local, 0, R.w, R.kt) + ds_part;
+      unsigned char *ds_dst = p.ds + cross_ds_tile(p, R.bh_local, R.w, R.kt) + ds_part;
       for (int j = 0; j < R.n; ++j, ++i, ds_dst += ds_step) {
         const uint32_t vec = sb + L::kOffVec + (i & 1) * 1024;
         bool w = mbar_wait(sb + BAR_VEC, i & 1, abort_flag, tmo, SITE_SOFTMAX);
@@ -620,8 +623,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_bwd_dkv_kernel(const __g
         }
       }
       if (!ok) break;
-      // ---- the segment's dV and dK: whole walks to the gradients, others to
-      // this CTA's first (the tile began before the run) or second slot
+      // ---- the segment's dV and dK: whole walks to the gradients (or the
+      // range's sums), others to this CTA's first (the tile began before the
+      // run) or second slot
       {
         const bool w = mbar_wait(sb + BAR_ACC, seg & 1, abort_flag, tmo, SITE_EPILOGUE);
         if (__any_sync(0xffffffffu, !w)) {
@@ -634,7 +638,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_bwd_dkv_kernel(const __g
         const int d0 = half * (D / 2);   // each half of the row writes half of the D columns
         float *part_dst = R.n < p.walk
                               ? p.partial + (static_cast<size_t>(blockIdx.x) * 2 + (R.w > 0 ? 0 : 1)) * (2 * 128 * D)
-                              : nullptr;
+                          : p.whole != nullptr ? p.whole + static_cast<size_t>(R.kt) * (2 * 128 * D)
+                                               : nullptr;
         for (int which = 0; which < 2; ++which) {   // 0: dV, 1: dK (times the softmax scale)
           const float mul = which == 0 ? 1.0f : p.scale;
           const uint32_t tsrc = (which == 0 ? tDV : tDK) + d0;
@@ -723,6 +728,45 @@ __device__ __forceinline__ void cross_join(const CrossBwdParams &p, int task, lo
   }
 }
 
+// A pair in ranges: each tile's sum over the ranges so far, the first range's
+// first, and after the last range the gradients.  A CTA a K tile, and dV or dK.
+template <int D>
+__global__ void __launch_bounds__(128) cross_range_kernel(const __grid_constant__ CrossBwdParams p) {
+  const int kt = static_cast<int>(blockIdx.x >> 1), which = static_cast<int>(blockIdx.x & 1), row = static_cast<int>(threadIdx.x);
+  const int b = p.by_hk.div(p.bh0), hk = p.bh0 - b * p.Hk;
+  const int n_kt = (cross_bwd_len(p, b) + 127) / 128;
+  if (kt >= n_kt) return;              // zeros, written beside the dQ product
+  const long long total = static_cast<long long>(n_kt) * p.walk, t0 = static_cast<long long>(kt) * p.walk;
+  // the runs first .. last share the tile (the quotient is that run or the one before it)
+  int first = static_cast<int>(t0 * p.ctas / total);
+  while (first + 1 < p.ctas && CrossRun::start(p, total, first + 1) <= t0) ++first;
+  int last = first;
+  while (last + 1 < p.ctas && CrossRun::start(p, total, last + 1) < t0 + p.walk) ++last;
+  const int k = kt * 128 + row;
+  for (int c = 0; c < D / 4; ++c) {
+    const size_t at = ((static_cast<size_t>(kt) * 2 + which) * (D / 4) + c) * 128 + row;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!p.first_range) a = reinterpret_cast<const float4 *>(p.sums)[at];
+    for (int r = first; r <= last; ++r) {
+      if (total < p.ctas && CrossRun::start(p, total, r) == CrossRun::start(p, total, r + 1)) continue;   // an empty run
+      const float4 v = first == last
+                           ? reinterpret_cast<const float4 *>(p.whole)[at]
+                           : reinterpret_cast<const float4 *>(p.partial)
+                                 [(((static_cast<size_t>(r) * 2 + (r == first ? 1 : 0)) * 2 + which) * (D / 4) + c) * 128 + row];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    if (!p.last_range)
+      reinterpret_cast<float4 *>(p.sums)[at] = a;
+    else if (k < p.Skv)
+      reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(which == 0 ? p.dv : p.dk) +
+                                ((static_cast<size_t>(b) * p.Skv + k) * p.Hk + hk) * D)[c] =
+          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+}
+
 // ============================================================== dQ product
 // dQ = dS K * scale, one CTA per SM walking (pair, head, Q tile) units; the
 // pipeline of attn_bwd_dq_gemm_kernel, with a third barrier per stage for the
@@ -775,18 +819,18 @@ __global__ void __launch_bounds__(kCrossGemmThreads, 1) cross_bwd_dq_kernel(cons
   const int units = p.n_bh * p.walk;                        // (head of the group, Q tile) units of the pairs
   const bool cleans = p.kv_lens != nullptr;
   struct Unit {
-    int b, hk, h, qt, len, n, bh_local, hg;
+    int b, hk, h, qt, len, n, bh_local, w;
   };
   auto unit_at = [&](int i) {
     Unit u;
     u.bh_local = p.by_walk.div(i);
-    const int r = i - u.bh_local * p.walk;
-    u.hg = p.by_q_tiles.div(r);
-    u.qt = r - u.hg * p.q_tiles;
+    u.w = i - u.bh_local * p.walk;
+    const int hg = p.by_q_tiles.div(p.w0 + u.w);
+    u.qt = p.w0 + u.w - hg * p.q_tiles;
     const int bh = p.bh0 + u.bh_local;
     u.b = p.by_hk.div(bh);
     u.hk = bh - u.b * p.Hk;
-    u.h = u.hk * group + u.hg;
+    u.h = u.hk * group + hg;
     u.len = cross_bwd_len(p, u.b);
     u.n = (u.len + 127) / 128;
     return u;
@@ -828,7 +872,7 @@ __global__ void __launch_bounds__(kCrossGemmThreads, 1) cross_bwd_dq_kernel(cons
       bool ok = true;
       for (int i = first; ok && i < units; i += step) {
         const Unit U = unit_at(i);
-        const unsigned char *a0 = p.ds + cross_ds_tile(p, U.bh_local, U.hg, U.qt, 0);
+        const unsigned char *a0 = p.ds + cross_ds_tile(p, U.bh_local, U.w, 0);
         for (int j = 0; j < U.n; ++j, ++it) {
           const int st = it % ST;
           if (!mbar_wait(sb + BAR_EMPTY + 8 * st, ((it / ST) & 1) ^ 1, abort_flag, tmo, SITE_PRODUCER)) {
@@ -884,7 +928,7 @@ __global__ void __launch_bounds__(kCrossGemmThreads, 1) cross_bwd_dq_kernel(cons
     }
   } else if (warp > 6) {
     // ------------------------------------------------------------ shared dK, dV tiles
-    for (int task = first; task < 2 * (p.ctas - 1); task += step)
+    for (int task = first; p.sums == nullptr && task < 2 * (p.ctas - 1); task += step)
       cross_join<D>(p, task, total, ends, static_cast<int>(threadIdx.x) - 224);
   } else if (warp == 6) {
     // ------------------------------------------------------------ K padding

@@ -195,6 +195,19 @@ static size_t cross_partial_bytes(int B, int H, int Hk, int Sq, int Skv, int D) 
   const double runs = std::min(static_cast<double>(kCrossMaxRuns), steps);
   return static_cast<size_t>(runs) * 2 * 2 * 128 * D * sizeof(float);
 }
+// dS of one pair, or where that is more than kCrossLeastDs, of a range of its
+// walk: as many steps as fit (a step takes 32 KB for each K tile, so there is
+// room for one).
+constexpr size_t kCrossLeastDs = size_t{256} << 20;
+static_assert(static_cast<size_t>(kCrossMaxKTiles) * kBwdDsTileBytes <= kCrossLeastDs, "a range of one step");
+static size_t cross_least_ds_bytes(int H, int Hk, int Sq, int Skv) {
+  return std::min(cross_pair_ds_bytes(H, Hk, Sq, Skv), kCrossLeastDs);
+}
+// The ranges' sums of dK and dV, and one range's of tiles that one run covers.
+static size_t cross_sums_bytes(int H, int Hk, int Sq, int Skv, int D) {
+  if (cross_pair_ds_bytes(H, Hk, Sq, Skv) <= kCrossLeastDs) return 0;
+  return static_cast<size_t>((Skv + 127) / 128) * 2 * 128 * D * sizeof(float);
+}
 
 // Delta: the self-attention's row sums where no element can have few states,
 // else the kernel that tells the elements apart.
@@ -276,6 +289,9 @@ static cudaError_t launch_cross_bwd_d(CrossBwdParams &p, cudaStream_t stream) {
   const int grid = std::min(std::max(units, 2 * (p.ctas - 1)), sms);
   cross_bwd_dq_kernel<D><<<static_cast<unsigned>(grid), kCrossGemmThreads,
                            CrossGemmSmem<D>::kAllocBytes + (p.kv_lens ? p.k_tiles * sizeof(int) : 0), stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.sums == nullptr) return e;
+  cross_range_kernel<D><<<static_cast<unsigned>(2 * p.k_tiles), 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -365,7 +381,7 @@ size_t cpattn_cross_attention_backward_ds_bytes(int H, int Hk, int Sq, int Skv) 
 size_t cpattn_cross_attention_backward_workspace_bytes(int B, int H, int Hk, int Sq, int Skv, int D) {
   if (check_cross_shape(B, H, Hk, Sq, Skv, D) != CPATTN_OK) return 0;
   return 256 + cross_delta_bytes(B, H, Sq) + cross_partial_bytes(B, H, Hk, Sq, Skv, D) +
-         cross_pair_ds_bytes(H, Hk, Sq, Skv);
+         2 * cross_sums_bytes(H, Hk, Sq, Skv, D) + cross_least_ds_bytes(H, Hk, Sq, Skv);
 }
 
 int cpattn_cross_attention_backward(const void *q, const long long *q_strides, const void *k,
@@ -405,10 +421,11 @@ int cpattn_cross_attention_backward(const void *q, const long long *q_strides, c
   base += cross_delta_bytes(B, H, Sq);
   p.partial = reinterpret_cast<float *>(base);
   base += cross_partial_bytes(B, H, Hk, Sq, Skv, D);
+  float *const sums = reinterpret_cast<float *>(base), *const whole = sums + cross_sums_bytes(H, Hk, Sq, Skv, D) / 4;
+  base += 2 * cross_sums_bytes(H, Hk, Sq, Skv, D);
   p.ds = base;
-  const size_t pair = cross_pair_ds_bytes(H, Hk, Sq, Skv);
+  const size_t pair = cross_pair_ds_bytes(H, Hk, Sq, Skv), space = static_cast<size_t>(end - base);
   const int pairs = B * Hk;
-  const int at_once = static_cast<int>(std::min<size_t>(static_cast<size_t>(pairs), static_cast<size_t>(end - base) / pair));
   p.lse = lse;
   p.delta = delta;
   p.kv_lens = kv_lens;
@@ -422,8 +439,7 @@ int cpattn_cross_attention_backward(const void *q, const long long *q_strides, c
   p.Hk = Hk;
   p.q_tiles = q_tiles;
   p.k_tiles = k_tiles;
-  p.walk = H / Hk * q_tiles;
-  p.by_walk.set(p.walk);
+  const int walk = H / Hk * q_tiles;
   p.by_hk.set(Hk);
   p.by_q_tiles.set(q_tiles);
   p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
@@ -431,14 +447,33 @@ int cpattn_cross_attention_backward(const void *q, const long long *q_strides, c
   p.timeout_ns = wait_timeout_ns();
   if (cudaError_t e = launch_cross_delta(p, q, vq, k, vk, v, vv, out, dout, delta, D, stream); e != cudaSuccess)
     return cuda_fail(e, "cross attention backward launch");
-  // Pairs whose dS fits together share the launches; the stream orders the
-  // next group after the product that read this one's dS.
-  for (int bh = 0; bh < pairs; bh += at_once) {
+  auto launch = [&](int bh, int n, int w0, int steps) {
     p.bh0 = bh;
-    p.n_bh = std::min(at_once, pairs - bh);
-    const cudaError_t e = D == 128 ? launch_cross_bwd_d<128>(p, stream) : launch_cross_bwd_d<64>(p, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "cross attention backward launch");
+    p.n_bh = n;
+    p.w0 = w0;
+    p.walk = steps;
+    p.by_walk.set(steps);
+    return D == 128 ? launch_cross_bwd_d<128>(p, stream) : launch_cross_bwd_d<64>(p, stream);
+  };
+  cudaError_t e = cudaSuccess;
+  if (space >= pair) {
+    // Pairs whose dS fits together share the launches; the stream orders the
+    // next group after the product that read this one's dS.
+    const int at_once = static_cast<int>(std::min<size_t>(static_cast<size_t>(pairs), space / pair));
+    for (int bh = 0; bh < pairs && e == cudaSuccess; bh += at_once) e = launch(bh, std::min(at_once, pairs - bh), 0, walk);
+  } else {
+    // Pair by pair in ranges of the walk whose dS fits.
+    const int at_once = static_cast<int>(space / (static_cast<size_t>(k_tiles) * kBwdDsTileBytes));
+    p.sums = sums;
+    p.whole = whole;
+    for (int bh = 0; bh < pairs; ++bh)
+      for (int w0 = 0; w0 < walk && e == cudaSuccess; w0 += at_once) {
+        p.first_range = w0 == 0;
+        p.last_range = walk - w0 <= at_once;
+        e = launch(bh, 1, w0, std::min(at_once, walk - w0));
+      }
   }
+  if (e != cudaSuccess) return cuda_fail(e, "cross attention backward launch");
   return CPATTN_OK;
 }
 

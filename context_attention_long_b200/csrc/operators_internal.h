@@ -113,10 +113,14 @@ struct alignas(64) CrossBwdParams {
   void *dq, *dk, *dv;                    // bf16, contiguous
   unsigned char *ds;                     // dS tiles of the pairs (cross_ds_tile), 256-byte aligned
   float *partial;                        // sums of tiles that runs share: [CTA][first, last tile][dV, dK][D / 4][128][4]
+  // A pair in ranges of its walk (one pair a launch; else null): the ranges'
+  // sums, and this range's of tiles that one run covers, both [K tile][dV, dK][D / 4][128][4]
+  float *sums, *whole;
+  int w0, first_range, last_range;       // first step of the range
   int B, Sq, Skv, H, Hk;
   int bh0, n_bh;
   int q_tiles, k_tiles;
-  int walk;                              // steps of a K/V tile: the Q tiles of its group's heads
+  int walk;                              // steps of a K/V tile: the Q tiles of its group's heads (or a range of them)
   int ctas;                              // runs that the valid tiles' walks are cut into
   double inv_ctas, inv_walk;
   FastDiv by_walk, by_hk, by_q_tiles;

@@ -653,11 +653,11 @@ int cpattn_cross_attention(const void *q, const long long *q_strides, const void
  *   workspace       device, any alignment, at least
  *                   cpattn_cross_attention_backward_workspace_bytes(): row sums,
  *                   float32 partial sums of dK and dV, and dS of one (batch
- *                   element, key head) pair, which is the least there is: 2
+ *                   element, key head) pair, or 256 MB of it: a pair whose dS
+ *                   does not fit is done in ranges of its queries.  Each
+ *                   cpattn_cross_attention_backward_ds_bytes() -- a pair's: 2
  *                   bytes a (query, state) of each of its H / Hk heads, both
- *                   lengths rounded up to 128 (17 GB for 32 / 4 heads, 32768
- *                   queries and as many states).  Each further
- *                   cpattn_cross_attention_backward_ds_bytes() lets one more
+ *                   lengths rounded up to 128 -- that fits lets one more
  *                   of the B * Hk pairs share the launches.  Overwritten;
  *                   calls that overlap on the GPU need one each.
  * rowsum(dout * out) is taken from the rounded out, except for elements of at

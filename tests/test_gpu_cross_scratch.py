@@ -75,3 +75,41 @@ def test_scratch_past_4_gb(Hk):
                                                     lse[:, one].contiguous(), dout[:, :, one].contiguous())[0]
         assert torch.equal(dq[:, :, one], alone)
     assert api.cpattn_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("B,Sq,H,Hk,D,Skv,lens,ranges", [
+    (1, 4100, 8, 1, 64, 4200, None, 2),
+    (1, 2300, 16, 1, 128, 4200, [4099], 2),
+    (2, 5000, 21, 3, 64, 6000, [6000, 129], 2),        # groups of seven, an element of few tiles
+    (2, 2400, 64, 2, 64, 4300, [0, 4300], 3),
+    (2, 1024, 8, 1, 64, 40000, [40000, 129], 3),       # a run covers whole tiles, and more runs than steps
+    (1, 1024, 8, 1, 128, 40000, None, 3),
+    (1, 16384, 8, 1, 64, 16640, None, 17),
+])
+def test_a_pair_in_ranges_of_its_queries(B, Sq, H, Hk, D, Skv, lens, ranges):
+    """The least workspace, which holds 256 MB of a pair's dS: dQ has the bytes
+    of whole pairs, dK and dV, which add the same terms in another order, differ
+    by their last rounding, and all of them are the same every run."""
+    pair = api.cpattn_cross_attention_backward_ds_bytes(H, Hk, Sq, Skv)
+    steps, q_tiles = (256 << 20) // ((Skv + 127) // 128 * 32768), (Sq + 127) // 128
+    assert -(-(H // Hk * q_tiles) // steps) == ranges
+    sizes = [api.cross_backward_workspace_bytes(B, H, Hk, Sq, Skv, D, ds_budget=n) for n in (0, 256 << 20, pair - 1, pair)]
+    assert sizes[0] == sizes[1] == sizes[2] - (pair - 1) + (256 << 20) == sizes[3] - pair + (256 << 20)
+    q, dout = normal(B, Sq, H, D, seed=1), normal(B, Sq, H, D, seed=4)
+    k, v = normal(B, Skv, Hk, D, seed=2), normal(B, Skv, Hk, D, seed=3)
+    n = lens_of(lens)
+    out, lse = api.cpattn_cross_attention(q, k, v, n)
+    args = (q, k, v, out, lse, dout, n)
+    whole = api.cpattn_cross_attention_backward(*args)
+    got = api.cpattn_cross_attention_backward(*args, ds_budget=0)
+    again = api.cpattn_cross_attention_backward(*args, ds_budget=0)
+    most = api.cpattn_cross_attention_backward(*args, ds_budget=pair - 1)     # all steps but one, then one
+    assert torch.equal(got[0], whole[0]) and torch.equal(most[0], whole[0])
+    for a, b, c, d in zip(got, again, most, whole):
+        assert torch.equal(a, b)
+        d = d.float()
+        for t in (a, c):     # a step of bf16, and float32's 2^-24 of the magnitudes where they cancel
+            assert bool(((t.float() - d).abs() <= 2.0 ** -7 * d.abs() + 2.0 ** -14 * d.abs().max()).all())
+    if Sq * Skv * H * B < 1 << 28:
+        check_norms(q, k, v, dout, [Skv] * B if lens is None else lens, got)
+    assert api.cpattn_device_status() == (0, 0)
