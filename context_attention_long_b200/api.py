@@ -667,23 +667,29 @@ def cross_backward_workspace_bytes(B, H, Hk, Sq, Skv, D, ds_budget=None) -> int:
     return cpattn_cross_attention_backward_workspace_bytes(B, H, Hk, Sq, Skv, D) + max(0, ds - least)
 
 
-# Scratch up to here is allocated without asking for the device's free memory, a
-# question of some 70 us of host time: a step with more takes longer on the GPU
-# than it does on the host, the question included.
+# Scratch up to here is allocated whatever the device's free memory.
 _CROSS_DS_UNASKED = 256 << 20
 
 
 def _cross_allocation_budget(device, every, ds_budget):
     """The dS budget for a workspace the cross-attention backward's binding
     allocates itself (`every`: dS of all pairs): the given one, or by default
-    BACKWARD_DS_BUDGET, what exceeds _CROSS_DS_UNASKED capped at half the
-    device's free memory."""
+    BACKWARD_DS_BUDGET, of which no more is newly taken from the device than
+    half its free memory.  Memory that torch holds and does not use, such as the
+    last step's scratch, is taken already; and the device is asked only for more
+    than that, since the question can stall for milliseconds where other
+    processes use the driver (training steps of 1.6 ms took 2 to 4 so, asked
+    every time)."""
     if ds_budget is not None:
         return int(ds_budget)
-    if min(every, BACKWARD_DS_BUDGET) <= _CROSS_DS_UNASKED:
-        return BACKWARD_DS_BUDGET
-    free, _ = torch.cuda.mem_get_info(device)
-    return min(BACKWARD_DS_BUDGET, max(_CROSS_DS_UNASKED, free // 2))
+    want = min(every, BACKWARD_DS_BUDGET)
+    if want > _CROSS_DS_UNASKED:
+        held = torch.cuda.memory_stats_as_nested_dict(device)
+        idle = held["reserved_bytes"]["all"]["current"] - held["allocated_bytes"]["all"]["current"]
+        if want > idle:
+            free, _ = torch.cuda.mem_get_info(device)
+            want = min(want, max(_CROSS_DS_UNASKED, idle, free // 2))
+    return want
 
 
 def cpattn_cross_attention_backward(q, k, v, out, lse, dout, kv_lens=None, dq=None, dk=None, dv=None, workspace=None,

@@ -103,19 +103,26 @@ def test_allocations_come_from_the_pool_of_the_launch_stream(host, i, stream):
 MB = 1 << 20
 
 
-@pytest.mark.parametrize("pair,free,ds_budget,pairs", [
-    (200 * MB, 100 << 30, None, 4),          # all there is
-    (200 * MB, 1000 * MB, None, 2),          # within half of what is free
-    (200 * MB, 300 * MB, None, 1),           # half is less than what is taken unasked: 256 MB, one pair
-    (200 * MB, 1000 * MB, 800 * MB, 4),      # the caller's own budget
-    (200 * MB, 1000 * MB, 0, 1),
-    (64 * MB, None, None, 4),                # 256 MB in all: the free memory is not asked for
+@pytest.mark.parametrize("pair,free,idle,ds_budget,pairs", [
+    (200 * MB, 100 << 30, 0, None, 4),          # all there is
+    (200 * MB, 1000 * MB, 0, None, 2),          # within half of what is free
+    (200 * MB, 300 * MB, 0, None, 1),           # half is less than what is always taken: 256 MB, one pair
+    (200 * MB, 300 * MB, 650 * MB, None, 3),    # or than what torch holds unused
+    (200 * MB, None, 800 * MB, None, 4),        # which is enough: the device is not asked
+    (200 * MB, None, 0, 800 * MB, 4),           # the caller's own budget
+    (200 * MB, None, 0, 0, 1),
+    (64 * MB, None, None, None, 4),             # 256 MB in all
 ])
-def test_scratch_of_the_cross_backward_leaves_free_memory(host, monkeypatch, pair, free, ds_budget, pairs):
+def test_scratch_of_the_cross_backward_leaves_free_memory(host, monkeypatch, pair, free, idle, ds_budget, pairs):
     def mem_get_info(device):
         assert free is not None
         return free, 180 << 30
+
+    def stats(device):
+        assert idle is not None
+        return {"reserved_bytes": {"all": {"current": 7 * MB + idle}}, "allocated_bytes": {"all": {"current": 7 * MB}}}
     monkeypatch.setattr(torch.cuda, "mem_get_info", mem_get_info)
+    monkeypatch.setattr(torch.cuda, "memory_stats_as_nested_dict", stats)
     monkeypatch.setattr(api, "cpattn_cross_attention_backward_ds_bytes", lambda *_: pair)
     monkeypatch.setattr(api, "cpattn_cross_attention_backward_workspace_bytes", lambda *_: 1000 + pair)
     q, k, lse = _host(2, 3, 4, 64), _host(2, 5, 2, 64), _host(2, 4, 3, dtype=torch.float32)
