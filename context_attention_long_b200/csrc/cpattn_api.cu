@@ -48,8 +48,8 @@ static_assert(sizeof(AttnParams) <= 32764, "AttnParams exceeds the kernel parame
 static_assert(sizeof(BwdParams) <= 32764, "BwdParams exceeds the kernel parameter limit");
 static_assert(sizeof(ProjParams) <= 32764, "ProjParams exceeds the kernel parameter limit");
 static_assert(sizeof(PermuteParams) <= 32764 && sizeof(MergeParams) <= 32764, "kernel parameter limit");
-static_assert(sizeof(NormRopeParams) <= 32764 && sizeof(CrossParams) <= 32764 &&
-                  sizeof(CrossBwdParams) <= 32764,
+static_assert(sizeof(NormRopeParams) <= 32764 && sizeof(CrossParams) <= 32764 && sizeof(CrossTokenParams) <= 32764 &&
+                  sizeof(CrossDeltaParams) <= 32764 && sizeof(CrossBwdParams) <= 32764,
               "kernel parameter limit");
 
 static unsigned long long wait_timeout_ns() {

@@ -5,7 +5,7 @@
 namespace cpattn {
 
 // 4-D view [B, rows, H, D] of a bf16 tensor, box {64, box_heads, box_rows,
-// 1}, 128-byte // swizzle; rows past the end of a batch element read as zero.
+// 1}, 128-byte swizzle; rows past the end of a batch element read as zero.
 static bool encode_view_map(CUtensorMap *tm, const void *ptr, int D, int H, int rows, int B, const View4 &v,
                             int box_rows = kQTile, int box_heads = 1) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -125,10 +125,13 @@ static cudaError_t launch_cross_d(CrossParams &p, cudaStream_t stream) {
 }
 
 // Few rows: the kernel of cross_token_kernel.cuh, up to 16 rows (query tokens
-// times heads of a group) a key head.  At 17 to 32 rows the tensor-core tiles
-// are as fast or faster (24 heads, 32 queries, 512 states: 9.3 us, with 32-row
-// fragments 10.3); at 16 and fewer they are not (8 requests, 32 / 8 heads, one
-// token, 1500 states: 14.5 us, with tiles 27.7).
+// times heads of a group) a key head, where it is faster (8 requests, 32 / 8
+// heads, one token, 1500 states: 14.5 us, with tiles 27.7).  At 32 rows of one
+// head and short states the tensor-core tiles are (24 heads, 32 queries, 512
+// states: 9.3 us, with 32-row fragments 10.3).  Against long states the step to
+// tiles costs: 4 x 24 heads, 4096 states, 16 queries take 36.8 us and 17 take
+// 60.6; most for groups whose heads do not share a tile (8 x 28 / 4 heads, 4096
+// states: 2 queries 13.0 us, 3 queries 58.4).
 constexpr int kTokenRows = 16;
 constexpr int kTokenSplits = 16;   // above the portable cluster size of 8: needs the kernel's opt-in
 
@@ -341,8 +344,11 @@ int cpattn_cross_attention(const void *q, const long long *q_strides, const void
   }
   CrossParams p;
   std::memset(&p, 0, sizeof(p));
-  // Heads of a group share tiles when a power of two of them divides a warp's
-  // 32 output rows and that takes fewer tiles (it never takes more).
+  // All heads of a group share tiles when their number is a power of two up to
+  // 32, so that whole queries make up a warp's 32 output rows; that never takes
+  // more tiles.  Heads of any other group have a tile each, however few their
+  // queries, and every pair of tiles walks the states again (8 x 64 / 1 heads,
+  // one query, 8192 states: 218 us, where 16 / 1 heads take 13).
   const int group = H / Hk;
   const bool pack = group <= 32 && (group & (group - 1)) == 0;
   const int heads = pack ? group : 1;

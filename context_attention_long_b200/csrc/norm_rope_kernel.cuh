@@ -14,10 +14,11 @@
 // HBM-bound: 4 bytes an element forward, 6 backward.  A row is D / 8 lanes
 // with one 16-byte piece each; a warp keeps one (tensor, block of heads) and
 // walks tokens, so that the weights stay in registers and a token's angles are
-// read once for all heads of the block; the loads of kU passes (with few
-// heads, of consecutive tokens) are issued before any is used.  dw: every lane sums its 8 columns over the rows of its
-// walk, then lanes, warps and CTAs are added in a fixed order (no atomics: the
-// same bytes every run), the CTAs' sums by a second small kernel.
+// read once for all heads of the block; the loads of kU passes (with few heads,
+// of consecutive tokens) are issued before any is used.  dw: every lane sums its
+// 8 columns over the rows of its walk, then lanes, warps and CTAs are added in a
+// fixed order (no atomics: the same bytes every run), the CTAs' sums by a second
+// small kernel.
 #pragma once
 
 #include "operators_internal.h"
