@@ -154,6 +154,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
+// Limit of the epilogue's waits, which last a unit's whole walk (the other roles
+// wait for a tile or two, and their giving up ends this wait too): 10 us more for
+// each of its n key tiles, which take 2.
+__device__ __forceinline__ uint64_t cross_walk_limit(uint64_t timeout_ns, int n) {
+  return timeout_ns + static_cast<uint64_t>(n) * 10000u;
+}
 // Every thread of every CTA of the cluster arrives and waits.
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -470,8 +476,9 @@ __global__ void __launch_bounds__(kCrossThreads, 1) cross_fwd_kernel(const __gri
       // MMAs read the K and V stages any more.
       const CrossUnit U = cross_unit<kSplit>(p, first);
       if (U.n > 0) {
-        bool w = mbar_wait(sb + BAR_O, 0, abort_flag, tmo, SITE_EPILOGUE);
-        if (U.two) w = w && mbar_wait(sb + BAR_O + 8, 0, abort_flag, tmo, SITE_EPILOGUE);
+        const uint64_t limit = cross_walk_limit(tmo, U.n);
+        bool w = mbar_wait(sb + BAR_O, 0, abort_flag, limit, SITE_EPILOGUE);
+        if (U.two) w = w && mbar_wait(sb + BAR_O + 8, 0, abort_flag, limit, SITE_EPILOGUE);
         ok = !__any_sync(0xffffffffu, !w);
         __syncwarp();
         tc_fence_after();
@@ -501,8 +508,9 @@ __global__ void __launch_bounds__(kCrossThreads, 1) cross_fwd_kernel(const __gri
         if (U.n > 0) {
           const uint32_t r = (rounds >> (16 * slot)) & 0xffffu;   // (its low two bits are used)
           rounds = slot == 0 ? (rounds & 0xffff0000u) | ((rounds + 1) & 0xffffu) : rounds + 0x10000u;
-          bool w = mbar_wait(sb + BAR_INV + 16 * slot + 8 * (r & 1), (r >> 1) & 1, abort_flag, tmo, SITE_EPILOGUE);
-          w = w && mbar_wait(sb + BAR_O + 8 * slot, r & 1, abort_flag, tmo, SITE_EPILOGUE);
+          const uint64_t limit = cross_walk_limit(tmo, U.n);
+          bool w = mbar_wait(sb + BAR_INV + 16 * slot + 8 * (r & 1), (r >> 1) & 1, abort_flag, limit, SITE_EPILOGUE);
+          w = w && mbar_wait(sb + BAR_O + 8 * slot, r & 1, abort_flag, limit, SITE_EPILOGUE);
           if (__any_sync(0xffffffffu, !w)) {
             ok = false;
             break;
