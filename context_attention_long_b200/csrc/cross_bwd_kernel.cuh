@@ -361,17 +361,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_bwd_dkv_kernel(const __g
       tma_prefetch_desc(&p.tm_v);
       tma_prefetch_desc(&p.tm_do);
       bool ok = true;
-      int i = 0, seg = 0;
-      for (; ok && R.left > 0; R.next(p), ++seg) {
-        if (!mbar_wait(sb + BAR_KVE, (seg & 1) ^ 1, abort_flag, tmo, SITE_PRODUCER)) break;
+      int i = 0, seg = 0;        // Q tiles and K/V tiles loaded
+      int o = 0;                 // dO tiles
+      while (ok && R.left > 0) {
+        ok = mbar_wait(sb + BAR_KVE, (seg & 1) ^ 1, abort_flag, tmo, SITE_PRODUCER);
+        if (!ok) break;
+        ++seg;
         mbar_arrive_expect_tx(sb + BAR_KV, 2 * L::kTileBytes);
         for (int hf = 0; hf < L::kHalves; ++hf) {
           tma_load_4d(sb + L::kOffA + hf * L::kBoxBytes, &p.tm_k, hf * 64, R.hk, R.kt * 128, R.b, sb + BAR_KV);
           tma_load_4d(sb + L::kOffB + hf * L::kBoxBytes, &p.tm_v, hf * 64, R.hk, R.kt * 128, R.b, sb + BAR_KV);
         }
         int hg = p.by_q_tiles.div(p.w0 + R.w), qt = p.w0 + R.w - hg * p.q_tiles;
-        for (int j = 0; j < R.n; ++j, ++i) {
-          const int qs = i % QS, os = i % OS;
+        for (int j = 0; j < R.n; ++j) {
+          const int qs = i % QS, os = o % OS;
           const int h = R.hk * group + hg;
           ok = mbar_wait(sb + BAR_QE + 8 * qs, ((i / QS) & 1) ^ 1, abort_flag, tmo, SITE_PRODUCER);
           if (!ok) break;
@@ -379,17 +382,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_bwd_dkv_kernel(const __g
           for (int hf = 0; hf < L::kHalves; ++hf)
             tma_load_4d(sb + L::kOffC + qs * L::kTileBytes + hf * L::kBoxBytes, &p.tm_q, hf * 64, h, qt * 128, R.b,
                         sb + BAR_QF + 8 * qs);
-          ok = mbar_wait(sb + BAR_OE + 8 * os, ((i / OS) & 1) ^ 1, abort_flag, tmo, SITE_PRODUCER);
+          ++i;
+          ok = mbar_wait(sb + BAR_OE + 8 * os, ((o / OS) & 1) ^ 1, abort_flag, tmo, SITE_PRODUCER);
           if (!ok) break;
           mbar_arrive_expect_tx(sb + BAR_OF + 8 * os, L::kTileBytes);
           for (int hf = 0; hf < L::kHalves; ++hf)
             tma_load_4d(sb + L::kOffE + os * L::kTileBytes + hf * L::kBoxBytes, &p.tm_do, hf * 64, h, qt * 128, R.b,
                         sb + BAR_OF + 8 * os);
+          ++o;
           if (++qt == p.q_tiles) {
             qt = 0;
             ++hg;
           }
         }
+        if (ok) R.next(p);
       }
       // every last release must arrive before the CTA exits
       if (ok) {
@@ -398,6 +404,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_bwd_dkv_kernel(const __g
         for (int j = 0; j < OS && j < i; ++j)
           mbar_wait(sb + BAR_OE + 8 * ((i - 1 - j) % OS), ((i - 1 - j) / OS) & 1, 0u, tmo, SITE_TAIL);
         if (seg > 0) mbar_wait(sb + BAR_KVE, (seg - 1) & 1, 0u, tmo, SITE_TAIL);
+      } else {   // a wait gave up: no CTA exits before what it loads has landed
+        if (seg > 0) mbar_wait(sb + BAR_KV, (seg - 1) & 1, 0u, tmo, SITE_TAIL);
+        for (int j = 0; j < QS && j < i; ++j)
+          mbar_wait(sb + BAR_QF + 8 * ((i - 1 - j) % QS), ((i - 1 - j) / QS) & 1, 0u, tmo, SITE_TAIL);
+        for (int j = 0; j < OS && j < o; ++j)
+          mbar_wait(sb + BAR_OF + 8 * ((o - 1 - j) % OS), ((o - 1 - j) / OS) & 1, 0u, tmo, SITE_TAIL);
       }
     }
   } else if (warp == 1) {

@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kCrossThreads, 1) cross_fwd_kernel(const __gri
   constexpr uint32_t TMEM_SLOT = L::kOffMisc;
   constexpr uint32_t ABORT = L::kOffMisc + 4;
   static_assert(BAR_TAIL + 8 <= L::kOffMisc, "barrier area");
+  static_assert((BAR_VF + 8 * NST - BAR_QF) / 8 <= 32, "the producer's masks");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -248,12 +249,16 @@ __global__ void __launch_bounds__(kCrossThreads, 1) cross_fwd_kernel(const __gri
         tma_prefetch_desc(&p.tm_v);
         int it = 0;              // K/V tiles loaded so far
         uint32_t q_used = 0, q_ph = 0;   // slots that loaded a Q tile, and the parity of the next load (a bit each)
+        uint32_t loaded = 0, last = 0;   // barriers from BAR_QF on that a load completes on, and its last load's parity
         bool ok = true;
         auto load = [&](uint32_t dst, const CUtensorMap *tm, int h, int row, int b, uint32_t full, uint32_t empty,
                         uint32_t use_parity) -> bool {
           if (!mbar_wait(empty, use_parity ^ 1, abort_flag, tmo, SITE_PRODUCER)) return false;
           mbar_arrive_expect_tx(full, L::kTileBytes);
           for (int hf = 0; hf < L::kHalves; ++hf) tma_load_4d(dst + hf * L::kBoxBytes, tm, hf * 64, h, row, b, full);
+          const uint32_t i = (full - sb - BAR_QF) >> 3;
+          loaded |= 1u << i;
+          last = (last & ~(1u << i)) | (use_parity << i);
           return true;
         };
         for (int unit = first; ok && unit < units; unit += step) {
@@ -292,6 +297,11 @@ __global__ void __launch_bounds__(kCrossThreads, 1) cross_fwd_kernel(const __gri
           }
           for (int s = 0; s < 2; ++s)
             if ((q_used >> s) & 1) mbar_wait(sb + BAR_QE + 8 * s, ((q_ph >> s) & 1) ^ 1, 0u, tmo, SITE_TAIL);
+        } else {   // a wait gave up: no CTA exits before what it loads has landed
+          for (; loaded != 0; loaded &= loaded - 1) {
+            const int i = __ffs(loaded) - 1;
+            mbar_wait(sb + BAR_QF + 8 * i, (last >> i) & 1, 0u, tmo, SITE_TAIL);
+          }
         }
       }
     } else if (warp == 1) {
