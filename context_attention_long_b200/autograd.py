@@ -72,13 +72,13 @@ def _readable(t):
 
 
 class _FirstOrderOnly(torch.autograd.Function):
-    """Passes a backward's gradients on as functions of `inputs` whose own
-    gradient raises."""
+    """Passes a backward's gradients, the first n of `tensors`, on as functions
+    of all of them whose own gradient raises."""
 
     @staticmethod
     def forward(ctx, name, n, *tensors):
-        ctx.name, ctx.n = name, n
-        return tensors[:n]
+        ctx.name = name
+        return tuple(t.detach() for t in tensors[:n])   # not the inputs themselves: views may not be changed in place
 
     @staticmethod
     def backward(ctx, *_):

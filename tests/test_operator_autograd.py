@@ -90,3 +90,21 @@ def test_recorded_gradients_may_go_unused(name):
     torch.testing.assert_close(other.grad, 36 * other.detach() ** 3)
     ordinary = torch.autograd.grad(f().sum(), leaves)
     assert not any(g.requires_grad for g in ordinary)
+
+
+@pytest.mark.parametrize("name", ["cross", "norm", "norm of one"])
+def test_recorded_gradients_may_be_changed_in_place(name):
+    """As clipping does."""
+    leaves, f, plain = _cases()[name]
+    want = torch.autograd.grad(plain().sum(), leaves)
+    f().sum().backward(create_graph=True)
+    with torch.no_grad():
+        for t in leaves:
+            t.grad.mul_(0.5)
+    for t, w in zip(leaves, want):
+        torch.testing.assert_close(t.grad.detach(), 0.5 * w, rtol=1e-9, atol=1e-9)
+    grads = torch.autograd.grad(f().sum(), leaves, create_graph=True)
+    for g, w in zip(grads, want):
+        torch.testing.assert_close(g.mul_(2).detach(), 2 * w, rtol=1e-9, atol=1e-9)
+    with pytest.raises(RuntimeError, match="not offered"):
+        sum(g.sum() for g in grads).backward()
